@@ -30,9 +30,10 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const __gri
     if (first) a.out_context_len[b] = ctx;
     return;
   }
-  const int rows = acc + 1;
-  ok = ok && acc >= 0 && rows <= hi - lo && rows <= kCommitMaxRows && (a.path == nullptr || acc <= a.max_depth) &&
-       ctx + int64_t(rows) <= room;
+  // (the accepted length before what is counted from it: the largest int has no successor)
+  ok = ok && acc >= 0 && acc < hi - lo && acc < kCommitMaxRows && (a.path == nullptr || acc <= a.max_depth) &&
+       ctx + int64_t(acc) < room;
+  const int rows = ok ? acc + 1 : 0;
   if (ok) {
     const int64_t* ns = kv ? a.vn_stride : a.kn_stride;
     const int64_t* cs = kv ? a.vc_stride : a.kc_stride;
