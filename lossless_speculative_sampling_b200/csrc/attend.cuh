@@ -262,14 +262,16 @@ __device__ bool attend_place(const AttendParams& p, AttendShared<DP>& sh, Attend
   constexpr int kWarps = kAttendThreads / 32;
   const int per = (p.B + kAttendThreads - 1) / kAttendThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int flags = 0;  // 1: error, 2: a pair of two tiles
+  int flags = 0;  // 1: bad offsets, 2: a pair of two tiles, 4: a bad length of the prefix
   AttendSize pre{0, 0, 0};
   int pre_len = 0;
   if (p.prefix_pages > 0) {
     const int nodes = __ldg(p.node_offsets + p.B);
     const AttendGroup g = load(-1);
-    if (g.bad || nodes < 0 || nodes > p.N) {
+    if (nodes < 0 || nodes > p.N) {
       flags |= 1;
+    } else if (g.bad) {
+      flags |= 4;
     } else {
       pre = group_size(g, p.shape);
       pre_len = g.len;
@@ -352,9 +354,10 @@ __device__ bool attend_place(const AttendParams& p, AttendShared<DP>& sh, Attend
     base.units = base_joined;
     load.pre_len = pre_len;
   }
-  const bool err = flags & 1;
+  // (bad offsets tell no rows apart: all N become NaN; of a bad prefix those of the requests)
+  const bool err = (flags & 5) != 0;
   if (blockIdx.x == 0 && tid == 0)
-    *p.plan = make_int4(err, shared, err ? p.N : __ldg(p.node_offsets + p.B), 0);
+    *p.plan = make_int4(err, shared, flags & 1 ? p.N : __ldg(p.node_offsets + p.B), 0);
   const int C = active_ctas(units, (flags & 2) != 0, p.ctas);
   *active = C;
   if (err || static_cast<int>(blockIdx.x) >= C) return false;

@@ -27,3 +27,26 @@ def test_commit_tree_accept_lengths_of_any_size(bad, path):
                               i32([[0, 1], [2, 3], [4, 5]]), i32([3, 3, 3]))
     assert new.tolist() == [6, -1, 6]
     assert torch.equal(kc, wk) and torch.equal(vc, wv)
+
+
+# --- trie attention ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens", [[5, 12], [64, 64, 40]])  # the prefix shared by all rows; read by each request
+@pytest.mark.parametrize("length,pages", [(-1, None), (49, None), (2**31 - 1, None), (33, -2), (33, 10**6)])
+def test_attend_tree_bad_prefix_leaves_rows_behind_alone(length, pages, lens):
+    """A prefix whose length or page is out of range makes every request's rows NaN; the rows behind the
+    last request stay as they were, as they do after a good call."""
+    p = Problem(lens, [40, 20, 7][:len(lens)], 33, 4, 2, 64, 16, torch.bfloat16, 62)
+    n, pad = sum(lens), 7
+    p.q, p.kn, p.vn = (torch.cat([t, torch.full_like(t[:pad], NAN)]) for t in (p.q, p.kn, p.vn))
+    p.parent += [-5] * pad
+    out, lse = torch.full((n + pad, 4, 64), 3.0, dtype=torch.bfloat16, device=DEV), torch.full((n + pad, 4), 3.0, device=DEV)
+    table = list(p.prefix_list)
+    if pages is not None:
+        table[1] = pages
+    p.call(prefix_pages=i32(table), prefix_len=i32([length]), out=out, lse=lse)
+    assert torch.isnan(out[:n]).all() and torch.isnan(lse[:n]).all()
+    assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()
+    p.off = [0, lens[0] + 1, lens[0]] + p.off[3:]  # bad offsets besides: no row is known to be behind
+    p.call(prefix_pages=i32(table), prefix_len=i32([length]), out=out, lse=lse)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
