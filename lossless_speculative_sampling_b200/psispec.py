@@ -418,8 +418,11 @@ def _on(device, stream):
     and the given stream (the current one if None), so that memory is taken from, and returns to,
     the stream that uses it."""
     if stream is not None:
-        return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
-                                 else torch.cuda.ExternalStream(int(stream), device=device))
+        if not hasattr(stream, "cuda_stream"):
+            # (of the handles 0 and 1, both the legacy default stream, torch makes a new stream or an error)
+            stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
+                      else torch.cuda.ExternalStream(int(stream), device=device))
+        return torch.cuda.stream(stream)
     if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
     return _HERE_AND_NOW

@@ -50,3 +50,43 @@ def test_attend_tree_bad_prefix_leaves_rows_behind_alone(length, pages, lens):
     p.off = [0, lens[0] + 1, lens[0]] + p.off[3:]  # bad offsets besides: no row is known to be behind
     p.call(prefix_pages=i32(table), prefix_len=i32([length]), out=out, lse=lse)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+# --- streams ----------------------------------------------------------------------------------
+
+def late(dst, src, stream):
+    """Fill dst on `stream`, behind tens of milliseconds of other work."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(1 << 26)
+        dst.copy_(src)
+
+
+@pytest.mark.parametrize("handle", [0, 1, "current", "default", "own"])
+def test_streams_by_handle(handle):
+    """A call runs on the stream that it is given, as a handle too: the legacy default stream has the
+    handles 0 and 1. It sees what was written there before it, and what follows there sees its results."""
+    s = torch.cuda.Stream() if handle == "own" else torch.cuda.default_stream()
+    h = {"current": torch.cuda.current_stream().cuda_stream, "own": s.cuda_stream, "default": s}.get(handle, handle)
+    p = Problem([5, 3], [40, 20], 33, 4, 2, 64, 16, torch.bfloat16, 63)
+    args, pre = p.args()
+    want = psispec.attend_tree(*args, **pre)
+    probs = torch.softmax(torch.randn(3, 500, generator=torch.Generator(DEV).manual_seed(64), device=DEV), -1)
+    off, x, ua, ur = i32([0, 2]), probs[:2].argmax(-1).int(), torch.zeros(2, device=DEV), torch.full((3,), 0.5, device=DEV)
+    ver = psispec.verify_probs(probs, None, off, x, ua, ur)
+    kc, vc = torch.zeros_like(p.kc), torch.zeros_like(p.vc)
+    page = (set(range(kc.shape[0])) - set(p.table[0][:3] + p.table[1][:2] + p.prefix_list)).pop()
+    table = i32([[page]])
+    q, k, rows = torch.zeros_like(args[0]), torch.zeros_like(args[1]), torch.full_like(probs, 1 / 500)
+    args[0], args[1], good_q, good_k = q, k, args[0], args[1]
+    zero, two = i32([0]), i32([2])
+    torch.cuda.synchronize()
+    for dst, src in ((q, good_q), (k, good_k), (rows, probs)):
+        late(dst, src, s)
+    a = psispec.attend_tree(*args, **pre, stream=h)
+    v = psispec.verify_probs(rows, None, off, x, ua, ur, stream=h)
+    n = psispec.commit_tree(k, args[2], args[3][:2], None, two, kc, vc, table, zero, stream=h)
+    with torch.cuda.stream(s):
+        got = [t.clone() for t in (a["out"], a["lse"], v["tokens"], v["accept_len"], n, kc[page, :3])]
+    torch.cuda.synchronize()
+    for g, w in zip(got, (want["out"], want["lse"], ver["tokens"], ver["accept_len"], i32([3]), good_k[:3])):
+        assert torch.equal(g, w)
