@@ -422,6 +422,8 @@ def _on(device, stream):
             # (of the handles 0 and 1, both the legacy default stream, torch makes a new stream or an error)
             stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
                       else torch.cuda.ExternalStream(int(stream), device=device))
+        elif getattr(stream, "device", device) != device:
+            raise ValueError("the stream is on %s, expected %s" % (stream.device, device))
         return torch.cuda.stream(stream)
     if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)

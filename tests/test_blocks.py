@@ -153,3 +153,12 @@ def test_binding_refuses_cpu_tensors():
         psispec.attend_tree(h, h, h, i, None, h, h, i, i)
     with pytest.raises(TypeError):
         psispec.commit_tree(h, h, i, None, i, h, h, i, i)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    """The kernels would run on that device, with addresses of the tensors' one."""
+    class Stream:
+        cuda_stream, device = 4096, torch.device("cuda", 1)
+
+    with pytest.raises(ValueError):
+        psispec._on(torch.device("cuda", 0), Stream())
