@@ -589,6 +589,8 @@ def commit_tree(k_nodes, v_nodes, node_offsets, path, accept_len, k_cache, v_cac
     pp, max_depth = 0, 0
     if path is not None:
         max_depth = path.shape[-1]
+        if max_depth == 0:  # (its address is null, which stands for the linear batch)
+            raise ValueError("path must have at least one column, or be None")
         pp = _ask(path, "path", torch.int32, B * max_depth, gpu)
     pa = _ask(accept_len, "accept_len", torch.int32, B, gpu)
     pt = _ask(page_table, "page_table", torch.int32, B * max_pages, gpu)

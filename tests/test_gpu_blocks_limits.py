@@ -90,3 +90,12 @@ def test_streams_by_handle(handle):
     torch.cuda.synchronize()
     for g, w in zip(got, (want["out"], want["lse"], ver["tokens"], ver["accept_len"], i32([3]), good_k[:3])):
         assert torch.equal(g, w)
+
+
+def test_commit_tree_refuses_a_path_without_columns():
+    """A path that holds no node is not the linear batch's missing path."""
+    kn, kc = torch.randn(4, 2, 64, device=DEV).bfloat16(), torch.zeros(2, 8, 2, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        psispec.commit_tree(kn, kn, i32([0, 4]), torch.zeros(1, 0, dtype=torch.int32, device=DEV), i32([2]), kc, kc.clone(),
+                            i32([[0]]), i32([0]))
+    assert (kc == 0).all()
