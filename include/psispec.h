@@ -425,7 +425,7 @@ typedef struct {
   int32_t dtype; /* PSISPEC_BF16 or PSISPEC_F16 */
   int32_t B, N, Hq, Hkv, D;
   int32_t pages, page_size, max_pages, prefix_pages;
-  float scale; /* > 0 */
+  float scale; /* > 0, at most 2^127 */
   const void* q;
   const void* k_nodes;
   const void* v_nodes;

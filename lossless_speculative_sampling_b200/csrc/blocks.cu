@@ -280,7 +280,7 @@ static psispec_status check_attend(const psispec_attend_tree_args* a) {
       a->pages <= 0 || a->page_size <= 0 || a->page_size % 8 != 0 || a->max_pages <= 0 || a->prefix_pages < 0)
     return PSISPEC_ERR_INVALID_ARG;
   if (a->prefix_pages > 0 && (!a->prefix_table || !a->prefix_len)) return PSISPEC_ERR_INVALID_ARG;
-  if (!(a->scale > 0.0f) || a->scale > 3.402823466e38f) return PSISPEC_ERR_INVALID_ARG;
+  if (!(a->scale > 0.0f) || a->scale > 0x1p127f) return PSISPEC_ERR_INVALID_ARG;  // (scale * log2(e) is finite)
   const int64_t qs[2] = {a->N, a->Hq}, ns[2] = {a->N, a->Hkv}, cs[3] = {a->pages, a->page_size, a->Hkv};
   if (bad_strides(a->q, a->q_stride, qs, 2, a->D) || bad_strides(a->k_nodes, a->kn_stride, ns, 2, a->D) ||
       bad_strides(a->v_nodes, a->vn_stride, ns, 2, a->D) || bad_strides(a->k_cache, a->kc_stride, cs, 3, a->D) ||

@@ -162,3 +162,12 @@ def test_binding_refuses_a_stream_of_another_device():
 
     with pytest.raises(ValueError):
         psispec._on(torch.device("cuda", 0), Stream())
+
+
+@pytest.mark.parametrize("scale", [3.0e38, 2.4e38])
+def test_attend_tree_refuses_scales_without_a_finite_logarithm_to_base_2(L, scale):
+    """Scores are kept in units of log 2: scale * log2(e) has to be finite too."""
+    a = _attend(scale=scale)
+    assert L.psispec_attend_tree(a, FAKE, 1 << 40, None) == psispec.ERR_INVALID_ARG
+    assert L.psispec_attend_tree_workspace(a) == 0
+    assert L.psispec_attend_tree_workspace(_attend(scale=2.0 ** 127)) > 0
