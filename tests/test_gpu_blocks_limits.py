@@ -1,5 +1,8 @@
 """GPU tests of the operators around a drafted block at the ends of what their arguments can hold,
 and of what a caller's own program does with them."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -99,3 +102,64 @@ def test_commit_tree_refuses_a_path_without_columns():
         psispec.commit_tree(kn, kn, i32([0, 4]), torch.zeros(1, 0, dtype=torch.int32, device=DEV), i32([2]), kc, kc.clone(),
                             i32([[0]]), i32([0]))
     assert (kc == 0).all()
+
+
+# --- a user's program ---------------------------------------------------------------------------
+
+def readme_step():
+    """The README's decoding step over candidate tries."""
+    with open(os.path.join(os.path.dirname(psispec.HEADER), "..", "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), flags=re.S)
+    return compile([b for b in blocks if "commit_tree(" in b][0], "README.md", "exec")
+
+
+@pytest.mark.parametrize("temp,top_p", [(0.0, 1.0), (0.7, 0.3), (0.7, 1.0), ("mixed", 0.5)])
+def test_the_readme_decodes(temp, top_p):
+    """Greedy requests and small top-p leave tries with unused slots, a draft row that is not finite leaves
+    none at all. Requests go on in every case but the last, and the last one alone stands still."""
+    g = torch.Generator(DEV).manual_seed(71)
+    B, K, V, n_prefixes, Hq, Hkv, D, page = 4, 4, 300, 12, 4, 2, 64, 16
+    emb = torch.randn(V, Hq * D, generator=g, device=DEV)
+    w = torch.randn(Hq * D, (Hq + 2 * Hkv) * D, generator=g, device=DEV) / 16
+    last_nodes = []
+
+    def qkv(tokens):
+        last_nodes.append(tokens)
+        return (emb[tokens.long()] @ w).bfloat16().view(-1, Hq + 2 * Hkv, D).split([Hq, Hkv, Hkv], 1)
+
+    def head(out):  # every node's likeliest next token: its own plus one, which is what is drafted
+        return (out.flatten(1).float() @ emb.T * 0.01 + 20.0 * torch.nn.functional.one_hot((last_nodes[-1].long() + 1) % V, V)).contiguous()
+
+    T = torch.tensor([0.0, 0.7, 0.0, 0.7] if temp == "mixed" else [temp] * B, device=DEV)
+    ns = dict(torch=torch, psispec=psispec, B=B, K=K, T=T, top_p=torch.full((B,), top_p, device=DEV), n_prefixes=n_prefixes,
+              cap=n_prefixes + 1, qkv=qkv, head=head, k_cache=torch.zeros(8, page, Hkv, D, dtype=torch.bfloat16, device=DEV),
+              page_table=i32([[2 * b, 2 * b + 1] for b in range(B)]), context_len=i32([0] * B), prompt_pages=None, prompt_len=None,
+              last_token=torch.randint(0, V, (B,), generator=g, device=DEV, dtype=torch.int32))
+    ns["v_cache"] = torch.zeros_like(ns["k_cache"])
+    history, step = [[int(t)] for t in ns["last_token"]], readme_step()
+    for it in range(3):
+        draft = torch.randn(B, K, V, generator=g, device=DEV)
+        for i in range(K):
+            draft[torch.arange(B), i, (ns["last_token"].long() + 1 + i) % V] += 12.0
+        if it == 2:
+            draft[3, 1, 7] = NAN
+        u = torch.rand(2, B * ns["cap"], generator=g, device=DEV)
+        old = ns["context_len"]
+        ns.update(draft=draft, u_acc=u[0], u_res=u[1])
+        exec(step, ns)
+        accepted, toks = ns["ver"]["accept_len"].tolist(), ns["ver"]["tokens"]
+        live = [b for b in range(B) if it < 2 or b != 3]
+        assert all(accepted[b] >= 0 for b in live) and (it < 2 or accepted[3] == -1)
+        assert ns["context_len"].tolist() == [c + a + 1 for c, a in zip(old.tolist(), accepted)]
+        for b in live:
+            history[b] += toks[b, :accepted[b] + 1].tolist()
+        ns["last_token"] = torch.tensor([h[-1] for h in history], dtype=torch.int32, device=DEV)
+    for b in range(B):  # the cache holds every token's keys but the last one's
+        n = int(ns["context_len"][b])
+        assert n == len(history[b]) - 1
+        want = qkv(torch.tensor(history[b][:n], device=DEV))[1]
+        got = ns["k_cache"][2 * b:2 * b + 2].flatten(0, 1)[:n]
+        # one rounding to bf16 each of sums of 256 products in fp32, in orders of their own
+        assert ((got.float() - want.float()).abs() <= 2.0**-7 * want.float().abs() + 2.0**-12).all()
+        if float(T[b]) == 0.0:  # greedy: whole blocks are accepted, 5 tokens a step
+            assert history[b] == [(history[b][0] + i) % V for i in range(len(history[b]))] and n >= 10
