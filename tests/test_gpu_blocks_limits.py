@@ -163,3 +163,98 @@ def test_the_readme_decodes(temp, top_p):
         assert ((got.float() - want.float()).abs() <= 2.0**-7 * want.float().abs() + 2.0**-12).all()
         if float(T[b]) == 0.0:  # greedy: whole blocks are accepted, 5 tokens a step
             assert history[b] == [(history[b][0] + i) % V for i in range(len(history[b]))] and n >= 10
+
+
+def test_a_step_of_the_tree_sampler_commits_the_right_rows():
+    """Four steps of a two-layer model with tries; every row of the cache, in both layers, against the
+    keys and values of the whole history run as one chain, and the same comparison with two rows of the cache
+    exchanged, which has to fail for every pair of neighbours and every layer.
+
+    Layer 0's keys and values are rows of a table by token: equal bit for bit, in the cache as in the chain.
+    Layer 1 sees x = emb + a, a the attention's output, with scores of a few units (a row's weight is
+    far from even). Of a, both runs are within u |a| + (1 + u) (u + 4 ds + 2^-20 + (2 n + 16) e) A <= 2.2 u A of the
+    exact one (u = 2^-8, |a| <= A = sum p |v| <= max |v|; scale sum |q k| is below 16 in layer 0, so 4 ds and the rest
+    are below u / 10), so they differ by 4.4 u max |v| at most, and their keys and values, products in fp64 rounded once,
+    by 4.4 u max |v| sum |w| + 2 u |k|. Layer 1's rows are of order 1 and differ by as much."""
+    g = torch.Generator(DEV).manual_seed(81)
+    B, K, V, Hq, Hkv, D, page, cap = 3, 4, 500, 4, 2, 64, 16, 11
+    u, E, dt = 2.0**-8, Hq * D, torch.bfloat16
+    emb = torch.randn(V, E, generator=g, device=DEV)
+    wq, wk, wv = ([torch.randn(E, h * D, generator=g, device=DEV).double() * (s / 16) for s in (1.0, 1.0)] for h in (Hq, Hkv, Hkv))
+    table0 = [(emb.double() @ w[0]).to(dt).view(V, -1, D) for w in (wq, wk, wv)]
+    q0, k0 = table0[0].abs().float(), table0[1].abs().float().repeat_interleave(Hq // Hkv, 1)
+    assert torch.einsum("ahd,bhd->abh", q0, k0).max() * D**-0.5 < 16
+
+    def run(tokens, off, parent, kc, vc, pages, ctx, pre):
+        """Both layers over nodes: the last layer's x, and the layers' keys and values."""
+        t, x = tokens.long(), emb[tokens.long()]
+        ks, vs = [], []
+        for layer in range(2):
+            q, k, v = ((tab[t] for tab in table0) if layer == 0 else
+                       ((x.double() @ w[1]).to(dt).view(len(t), -1, D) for w in (wq, wk, wv)))
+            ks.append(k.contiguous())
+            vs.append(v.contiguous())
+            r = psispec.attend_tree(q.contiguous(), ks[-1], vs[-1], off, parent, kc[layer], vc[layer], pages, ctx,
+                                    prefix_pages=pre[0], prefix_len=pre[1])
+            x = x + r["out"].float().reshape(x.shape)
+        return x, torch.stack(ks), torch.stack(vs)
+
+    kc, vc = (torch.full((2, 40, page, Hkv, D), NAN, dtype=dt, device=DEV) for _ in range(2))
+    prompt, none = torch.randint(0, V, (40,), generator=g, device=DEV), (None, None)
+    ppages = i32([[5, 17, 2]])
+    _, k, v = run(prompt, i32([0, 40]), None, kc, vc, ppages, i32([0]), none)
+    assert psispec.commit_tree(k, v, i32([0, 40]), None, i32([39]), kc, vc, ppages, i32([0])).tolist() == [40]
+    pre, pages = (ppages[0].contiguous(), i32([40])), i32([[20 + b, 30 + b] for b in range(B)])
+    ctx, root = i32([0] * B), torch.randint(0, V, (B,), generator=g, device=DEV, dtype=torch.int32)
+    T, P = torch.full((B,), 0.7, device=DEV), torch.ones(B, device=DEV)
+    history = [prompt.tolist() + [int(r)] for r in root]
+    for _ in range(4):
+        tr = psispec.build_tree((torch.randn(B, K, V, generator=g, device=DEV) * 3).contiguous(), T, P, 4, cap - 1)
+        assert tr["nodes"].tolist() == [cap] * B
+        tokens = tr["tokens"].clone()
+        tokens[:, 0] = root
+        off, parent, flat = offsets([cap] * B), tr["parent"].reshape(-1).contiguous(), tokens.reshape(-1)
+        _, k, v = run(flat, off, parent, kc, vc, pages, ctx, pre)
+        # the model's own logits do not matter here: a node's children are far likelier than other tokens
+        logits = torch.randn(B, cap, V, generator=g, device=DEV)
+        at = (torch.arange(B, device=DEV)[:, None], tr["parent"][:, 1:].long(), tokens[:, 1:].long())
+        logits[at] += 12.0
+        logits = logits.view(B * cap, V)
+        un = torch.rand(2, B * cap, generator=g, device=DEV)
+        out = psispec.verify_tree_det(logits, off, parent, flat.contiguous(), un[0].contiguous(), un[1].contiguous(), T, P, K)
+        ctx = psispec.commit_tree(k, v, off, out["path"], out["accept_len"], kc, vc, pages, ctx)
+        for b in range(B):
+            history[b] += out["tokens"][b, :int(out["accept_len"][b]) + 1].tolist()
+        root = out["tokens"].gather(1, out["accept_len"].long()[:, None])[:, 0]
+    assert int((ctx - 4).sum()) >= 4  # nodes behind the roots were accepted
+
+    def excess(kc, vc, b):
+        """How far each layer's rows of request b, prompt included, are beyond the bound: [2, rows], at most 0."""
+        n = 40 + int(ctx[b])
+        h = torch.tensor(history[b], device=DEV)
+        assert len(h) == n + 1
+        _, *want = run(h[:n], i32([0, n]), None, kc, vc, i32([[0]]), i32([0]), none)
+        most = want[1][0].float().abs().max()
+        worst = torch.full((2, n), -1.0, device=DEV)
+        for cache, w1, wt in ((kc, wk, want[0]), (vc, wv, want[1])):
+            got = torch.cat([cache[:, ppages[0].long()].flatten(1, 2)[:, :40], cache[:, pages[b].long()].flatten(1, 2)[:, :n - 40]], 1)
+            d = (got.float() - wt.float()).abs()
+            bound = torch.zeros_like(d)
+            bound[1] = 4.4 * u * most * w1[1].abs().sum(0).float().view(Hkv, D) + 2 * u * wt[1].float().abs()
+            worst = torch.maximum(worst, (d - bound).flatten(2).amax(-1))
+        return worst
+
+    for b in range(B):
+        right = excess(kc, vc, b)
+        assert (right <= 0).all(), float(right.max())
+        own = int(ctx[b])
+        for layer in range(2):
+            for i in range(own - 1):
+                if history[b][40 + i] == history[b][41 + i]:
+                    continue
+                k2, v2 = kc.clone(), vc.clone()
+                at = [(int(pages[b, j // page]), j % page) for j in (i, i + 1)]
+                for c2, c in ((k2, kc), (v2, vc)):
+                    c2[layer][at[0]], c2[layer][at[1]] = c[layer][at[1]], c[layer][at[0]]
+                wrong = excess(k2, v2, b)
+                assert (wrong[layer, 40 + i:42 + i] > 0).all() and (wrong[1 - layer] <= 0).all()
