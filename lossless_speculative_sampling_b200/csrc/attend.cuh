@@ -52,6 +52,15 @@ constexpr int kAttendThreads = 384;
 constexpr int kSoftmaxRegs = 208, kHelperRegs = 88;
 constexpr float kRaise = 8.0f;  // log2 of how far weights may pass 1 before the maximum is raised
 
+// What a wait inside the kernel is given (about a second), and whether the ancestors of node tiles are handed
+// over: a build for tests lowers the one and leaves out the other, so that waits run out.
+#ifndef PSISPEC_ATTEND_WAIT_CYCLES
+#define PSISPEC_ATTEND_WAIT_CYCLES (1ll << 31)
+#endif
+#ifndef PSISPEC_ATTEND_HAND_OVER
+#define PSISPEC_ATTEND_HAND_OVER 1
+#endif
+
 template <int DP>
 struct AttendCfg {
   static constexpr int kHalves = DP / 64;                          // 64-column (128-byte) swizzled blocks of a tile
@@ -216,13 +225,15 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return d;
 }
 
-// Bounded wait: gives up after about a second (2^31 cycles), or as soon as another role has given up.
+// Bounded wait: gives up after PSISPEC_ATTEND_WAIT_CYCLES, or as soon as another role has given up. A role that gives up
+// leaves its loop; copies and products that were issued are waited for (with a limit) by the warps that issued them,
+// and the second kernel makes all rows NaN.
 __device__ __forceinline__ bool attend_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (*dead) return false;
-    if (clock64() - t0 > (1ll << 31)) {
+    if (clock64() - t0 > PSISPEC_ATTEND_WAIT_CYCLES) {
       *dead = 1;
       return false;
     }
@@ -791,7 +802,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
               if (lane == 0) sh.bad_node[s][buf][k] = word;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.n_full[s][buf]);
+            if (PSISPEC_ATTEND_HAND_OVER && lane == 0) mbar_arrive(&sh.n_full[s][buf]);
           }
         }
         if (!ok) break;
@@ -888,12 +899,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
         if (lane == 0) mbar_arrive(&sh.w_empty[at % kWorkRing]);
         ++at;
       }
-      if (!ok) {  // gave up: no copy may still land when the CTA leaves
-        for (int i = 0; i < 2; ++i)
-          if (q_uses[i]) mbar_wait_bounded(&sh.q_full[i], (q_uses[i] - 1) & 1);
-        for (int i = max(slots - Cfg::kStages, 0); i < slots; ++i)
-          mbar_wait_bounded(&sh.kv_full[i % Cfg::kStages], (i / Cfg::kStages) & 1);
-      }
+      // no copy may still land when the CTA leaves; where another role gives up, even later than here, nobody
+      // else has waited for the last ones
+      for (int i = 0; i < 2; ++i)
+        if (q_uses[i]) mbar_wait_bounded(&sh.q_full[i], (q_uses[i] - 1) & 1);
+      for (int i = max(slots - Cfg::kStages, 0); i < slots; ++i)
+        mbar_wait_bounded(&sh.kv_full[i % Cfg::kStages], (i / Cfg::kStages) & 1);
     } else if (warp == 8) {
       // ----- matrix products -----
       constexpr uint32_t fmt = F16 ? 0u : 1u;

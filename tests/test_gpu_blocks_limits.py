@@ -1,11 +1,14 @@
 """GPU tests of the operators around a drafted block at the ends of what their arguments can hold,
 and of what a caller's own program does with them."""
+import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
 
+from lossless_speculative_sampling_b200 import build as libbuild
 from lossless_speculative_sampling_b200 import psispec
 from test_gpu_blocks import DEV, Problem, i32, offsets
 
@@ -258,3 +261,40 @@ def test_a_step_of_the_tree_sampler_commits_the_right_rows():
                     c2[layer][at[0]], c2[layer][at[1]] = c[layer][at[1]], c[layer][at[0]]
                 wrong = excess(k2, v2, b)
                 assert (wrong[layer, 40 + i:42 + i] > 0).all() and (wrong[1 - layer] <= 0).all()
+
+
+# --- what no argument reaches: a library built with other limits ----------------------------------
+
+def limited_library(tmp_path, *defines):
+    """The operators built with lower limits, loaded beside the library that the other tests use."""
+    so = str(tmp_path / "limited.so")
+    subprocess.check_call([libbuild.NVCC] + libbuild.FLAGS + ["-D" + d for d in defines]
+                          + ["-o", so, os.path.join(libbuild.CSRC, "blocks.cu")])
+    lib, real = ctypes.CDLL(so), psispec.lib()
+    for f in ("psispec_attend_tree", "psispec_attend_tree_workspace"):
+        getattr(lib, f).argtypes, getattr(lib, f).restype = getattr(real, f).argtypes, getattr(real, f).restype
+    return lib
+
+
+def test_attend_tree_waits_that_run_out(tmp_path, monkeypatch):
+    """With node tiles that are never handed over and waits of 2^22 cycles (two milliseconds) the kernels end,
+    copies in flight or not, with every row of the requests NaN and the rows behind them as they were, those
+    included that were written at once or by CTAs that had no node tile. The next call on the same
+    workspace is right."""
+    lib = limited_library(tmp_path, "PSISPEC_ATTEND_WAIT_CYCLES=(1ll<<22)", "PSISPEC_ATTEND_HAND_OVER=0")
+    for lens, ctx, prefix, heads in (([5, 1, 12], [300, 0, 2000], 33, (4, 2, 64)), ([64, 33, 61], [100, 700, 0], 500, (8, 2, 128)),
+                                     ([1] * 9, [3000] * 9, 64, (8, 2, 64)), ([40] * 90, [200] * 90, 0, (8, 2, 64))):
+        p = Problem(lens, ctx, prefix, *heads, 16, torch.bfloat16, 91)
+        n, pad = sum(lens), 3
+        p.q, p.kn, p.vn = (torch.cat([t, torch.full_like(t[:pad], NAN)]) for t in (p.q, p.kn, p.vn))
+        p.parent += [0] * pad
+        out = torch.full((n + pad, heads[0], heads[2]), 3.0, dtype=torch.bfloat16, device=DEV)
+        lse, ws = torch.full((n + pad, heads[0]), 3.0, device=DEV), torch.zeros(1 << 26, dtype=torch.uint8, device=DEV)
+        with monkeypatch.context() as m:
+            m.setattr(psispec, "_lib", lib)
+            p.call(out=out, lse=lse, ws=ws)
+            torch.cuda.synchronize()
+        assert torch.isnan(out[:n]).all() and torch.isnan(lse[:n]).all()
+        assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()
+        p.check(p.call(out=out, lse=lse, ws=ws))
+        assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()
