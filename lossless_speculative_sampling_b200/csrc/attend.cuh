@@ -60,6 +60,12 @@ constexpr float kRaise = 8.0f;  // log2 of how far weights may pass 1 before the
 #ifndef PSISPEC_ATTEND_HAND_OVER
 #define PSISPEC_ATTEND_HAND_OVER 1
 #endif
+// The most ancestors of a node: they are followed one by one, up to four times for a tile, and the wait for
+// them has to see their end (4 x 2^18 steps of up to 2000 cycles, several times what a load takes). Lower
+// in a build for tests.
+#ifndef PSISPEC_ATTEND_MAX_DEPTH
+#define PSISPEC_ATTEND_MAX_DEPTH (1 << 18)
+#endif
 
 template <int DP>
 struct AttendCfg {
@@ -402,7 +408,7 @@ __device__ bool attend_place(const AttendParams& p, AttendShared<DP>& sh, Attend
 }
 
 // Bits of the nodes of key tile `base` (request-local nodes base .. base + 127) that node i sees:
-// itself and its ancestors. False if a parent is out of range.
+// itself and its ancestors. False if a parent is out of range or there are too many.
 __device__ __forceinline__ bool ancestor_bits(const int32_t* parent, int i, int base, uint32_t (&bits)[4]) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) bits[w] = 0;
@@ -414,7 +420,7 @@ __device__ __forceinline__ bool ancestor_bits(const int32_t* parent, int i, int 
     }
     return true;
   }
-  while (i >= base) {
+  for (int steps = 0; i >= base; ++steps) {
     const int k = i - base;
     if (k < kTileKeys) {
 #pragma unroll
@@ -422,7 +428,7 @@ __device__ __forceinline__ bool ancestor_bits(const int32_t* parent, int i, int 
         if ((k >> 5) == w) bits[w] |= 1u << (k & 31);
     }
     const int up = __ldg(parent + i);
-    if (up < -1 || up >= i) return false;
+    if (up < -1 || up >= i || (up >= 0 && steps == PSISPEC_ATTEND_MAX_DEPTH)) return false;
     i = up;
   }
   return true;

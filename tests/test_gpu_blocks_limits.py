@@ -298,3 +298,24 @@ def test_attend_tree_waits_that_run_out(tmp_path, monkeypatch):
         assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()
         p.check(p.call(out=out, lse=lse, ws=ws))
         assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()
+
+
+def test_attend_tree_depth(tmp_path, monkeypatch):
+    """A node with more ancestors than the limit is a data error of its rows (here beyond 200, of one chain by
+    parents across tiles and of a shallow trie of as many nodes); a chain without parents has no limit."""
+    lib = limited_library(tmp_path, "PSISPEC_ATTEND_MAX_DEPTH=200")
+    n = 450
+    chain = [i - 1 for i in range(n)]
+    shallow = [-1] + [(i - 1) // 2 for i in range(1, n)]
+    p = Problem([n, n, 40], [30, 0, 300], 50, 4, 2, 64, 16, torch.bfloat16, 92, parents=chain + shallow + chain[:40])
+    with monkeypatch.context() as m:
+        m.setattr(psispec, "_lib", lib)
+        r = p.call()
+        torch.cuda.synchronize()
+    assert torch.isnan(r["out"][201:n]).all() and torch.isnan(r["lse"][201:n]).all()
+    p.check(r, rows={0: slice(0, 201)})
+    p.check()
+    p.parent = None
+    with monkeypatch.context() as m:
+        m.setattr(psispec, "_lib", lib)
+        p.check()
