@@ -52,14 +52,18 @@ constexpr int kAttendThreads = 384;
 constexpr int kSoftmaxRegs = 208, kHelperRegs = 88;
 constexpr float kRaise = 8.0f;  // log2 of how far weights may pass 1 before the maximum is raised
 
-// What a wait inside the kernel is given (about a second), and whether the ancestors of node tiles are handed
-// over: a build for tests lowers the one and leaves out the other, so that waits run out.
+// What a wait inside the kernel is given (about a second), besides kUnitCycles for every unit of its CTA's work, and
+// whether the ancestors of node tiles are handed over: a build for tests lowers the one and leaves out the
+// other, so that waits run out.
 #ifndef PSISPEC_ATTEND_WAIT_CYCLES
 #define PSISPEC_ATTEND_WAIT_CYCLES (1ll << 31)
 #endif
 #ifndef PSISPEC_ATTEND_HAND_OVER
 #define PSISPEC_ATTEND_HAND_OVER 1
 #endif
+// A unit takes up to 2000 cycles; the parts that run ahead of the tiles wait for whole segments of them, which may
+// take longer than a second.
+constexpr long long kUnitCycles = 1 << 14;
 // The most ancestors of a node: they are followed one by one, up to four times for a tile, and the wait for
 // them has to see their end (4 x 2^18 steps of up to 2000 cycles, several times what a load takes). Lower
 // in a build for tests.
@@ -119,6 +123,12 @@ struct AttendWork {
 };
 constexpr int kWorkRing = 4;
 
+// What every wait looks at: whether a role has given up, and when to.
+struct AttendGuard {
+  volatile int dead;
+  long long limit;
+};
+
 template <int DP>
 struct AttendShared {
   uint64_t q_full[2], q_empty[2], kv_full[AttendCfg<DP>::kStages], kv_empty[AttendCfg<DP>::kStages];
@@ -132,7 +142,7 @@ struct AttendShared {
   uint32_t not_finite[2][2][2][4];  // per width of the pair and stream, alternating: value rows of a node tile
                                     // that are not finite
   uint32_t tmem;
-  volatile int dead;
+  AttendGuard guard;
 };
 
 template <int DP>
@@ -231,16 +241,16 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return d;
 }
 
-// Bounded wait: gives up after PSISPEC_ATTEND_WAIT_CYCLES, or as soon as another role has given up. A role that gives up
+// Bounded wait: gives up after the guard's limit, or as soon as another role has given up. A role that gives up
 // leaves its loop; copies and products that were issued are waited for (with a limit) by the warps that issued them,
 // and the second kernel makes all rows NaN.
-__device__ __forceinline__ bool attend_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ bool attend_wait(uint64_t* bar, uint32_t parity, AttendGuard* guard) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
-    if (*dead) return false;
-    if (clock64() - t0 > PSISPEC_ATTEND_WAIT_CYCLES) {
-      *dead = 1;
+    if (guard->dead) return false;
+    if (clock64() - t0 > guard->limit) {
+      guard->dead = 1;
       return false;
     }
   }
@@ -437,7 +447,7 @@ __device__ __forceinline__ bool ancestor_bits(const int32_t* parent, int i, int 
 // A softmax warp: rows 32 wq .. 32 wq + 31 of stream s, one per lane.
 template <int DP, bool F16>
 __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShared<DP>& sh, uint8_t* tiles, uint32_t tmem,
-                                               volatile int* dead) {
+                                               AttendGuard* guard) {
   using Cfg = AttendCfg<DP>;
   const int G = p.shape.G, npt = p.shape.npt;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -451,7 +461,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
   bool ok = true;
   for (int at = 0;; ++at) {
     const AttendWork& w = sh.work[at % kWorkRing];
-    ok = __all_sync(0xffffffffu, attend_wait(&sh.w_full[at % kWorkRing], (at / kWorkRing) & 1, dead));
+    ok = __all_sync(0xffffffffu, attend_wait(&sh.w_full[at % kWorkRing], (at / kWorkRing) & 1, guard));
     if (!ok || w.last) break;
     const bool wide = w.wide;
     const int n = w.tiles, steps = wide ? n : (n + 1 - s) / 2;
@@ -471,7 +481,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
       uint32_t bits[4];
       if (is_node) {
         const int buf = n_uses & 1;
-        ok = __all_sync(0xffffffffu, attend_wait(&sh.n_full[s][buf], (n_uses >> 1) & 1, dead));
+        ok = __all_sync(0xffffffffu, attend_wait(&sh.n_full[s][buf], (n_uses >> 1) & 1, guard));
         if (!ok) break;
         ++n_uses;
         const uint4 x4 = p.seen[((blockIdx.x * 2 + s) * 2 + buf) * kTileRows + node_in];
@@ -487,7 +497,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
           bits[j] = k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
         }
       }
-      ok = __all_sync(0xffffffffu, attend_wait(&sh.s_full[s], s_uses & 1, dead));
+      ok = __all_sync(0xffffffffu, attend_wait(&sh.s_full[s], s_uses & 1, guard));
       if (!ok) break;
       ++s_uses;
       tmem_fence_after();
@@ -550,7 +560,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
       }
       if (is_node || count < kTileKeys) {  // rows of V that must not be multiplied
         const int slot = w.ring + v_slot(wide, tt, n), st = slot % Cfg::kStages;
-        ok = __all_sync(0xffffffffu, attend_wait(&sh.kv_full[st], (slot / Cfg::kStages) & 1, dead));
+        ok = __all_sync(0xffffffffu, attend_wait(&sh.kv_full[st], (slot / Cfg::kStages) & 1, guard));
         if (!ok) break;
         uint8_t* const row = tiles + (2 + st) * Cfg::kTileBytes + r * 128;
         bool drop = r >= count;
@@ -575,7 +585,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
             sh.not_finite[wide][s][buf][wq] = word;
             mbar_arrive(met);
           }
-          ok = __all_sync(0xffffffffu, attend_wait(met, use & 1, dead));
+          ok = __all_sync(0xffffffffu, attend_wait(met, use & 1, guard));
           if (!ok) break;
           ++v_uses[wide];
           const volatile uint32_t* mine = sh.not_finite[wide][s][buf];
@@ -603,7 +613,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
     const int64_t slot_row = w.row + (s ? w.rows[0] : 0) + r;
     const int64_t out_row = int64_t(w.lo + node) * p.Hq + w.kvh * G + head_in;  // of a wide pair
     if (steps > 0) {
-      ok = __all_sync(0xffffffffu, attend_wait(&sh.o_full[s], o_uses & 1, dead));
+      ok = __all_sync(0xffffffffu, attend_wait(&sh.o_full[s], o_uses & 1, guard));
       if (!ok) break;
       ++o_uses;
       tmem_fence_after();
@@ -664,7 +674,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   AttendShared<DP>& sh = *reinterpret_cast<AttendShared<DP>*>(tiles + Cfg::kTiles * Cfg::kTileBytes);
   const uint32_t q_addr = smem_u32(tiles), kv_addr = q_addr + 2 * Cfg::kTileBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  volatile int* dead = &sh.dead;
+  AttendGuard* const guard = &sh.guard;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -690,7 +700,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
     mbar_init(&sh.v_one[0], 4);
     mbar_init(&sh.v_one[1], 4);
     mbar_init(&sh.done, 1);
-    sh.dead = 0;
+    sh.guard.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -699,6 +709,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   AttendWalk walk;
   int C = 0;
   if (!attend_place<DP>(p, sh, load, walk, &C)) return;  // the same in every thread
+  if (tid == 0) sh.guard.limit = PSISPEC_ATTEND_WAIT_CYCLES + (walk.w1 - walk.w0) * kUnitCycles;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
                  : "memory");
@@ -713,7 +724,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   bool ok = true;
   // the next segment, null at the end
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, attend_wait(bar, parity, dead)) != 0;
+    return __all_sync(0xffffffffu, attend_wait(bar, parity, guard)) != 0;
   };
   auto take = [&]() -> const AttendWork* {
     const int i = at % kWorkRing;
@@ -986,12 +997,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   } else {
     // ----- softmax -----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    attend_softmax<DP, F16>(p, sh, tiles, tmem, dead);
+    attend_softmax<DP, F16>(p, sh, tiles, tmem, guard);
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (tid == 0 && sh.dead) p.plan->w = 1;  // gave up: the second kernel answers NaN
+  if (tid == 0 && sh.guard.dead) p.plan->w = 1;  // gave up: the second kernel answers NaN
   if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
