@@ -418,10 +418,10 @@ psispec_status psispec_verify_probs(const void* target_probs, int64_t target_str
  * [0, max_pages * page_size] or a page outside [0, pages) in that request (of the prefix: in every
  * request); offsets out of order in all N rows. A value of a node's v_nodes that is not finite
  * reaches the rows of that node and its descendants alone (it may turn them into NaN as a whole).
- * One outcome is no data error: the kernel's parts wait for one another with a limit (about a second, and
- * more for more work: eight times what a block's share takes), so that a fault of the device or of
- * this library cannot hang it. If a limit passes, all rows of all requests become NaN; the call itself has
- * returned PSISPEC_OK by then.
+ * One outcome is no data error: the kernel's parts wait for one another with a limit (about a second; for
+ * whole stretches of work eight times what they take besides), so that a fault of the device or of this
+ * library cannot hang it. If a limit passes, all rows of all requests become NaN; the call itself has returned
+ * PSISPEC_OK by then.
  * Limits: D a multiple of 8 up to 128, Hq / Hkv up to 128, Hkv up to 1024, page_size a multiple of 8,
  * N * Hq <= 2^22, B <= 2^20, tokens of a page table's row <= 2^30; a node with more than 2^18 ancestors counts
  * as one with a bad parent. Ancestors in parent are followed one by one: a long chain is faster with

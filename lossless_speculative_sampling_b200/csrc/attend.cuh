@@ -52,17 +52,17 @@ constexpr int kAttendThreads = 384;
 constexpr int kSoftmaxRegs = 208, kHelperRegs = 88;
 constexpr float kRaise = 8.0f;  // log2 of how far weights may pass 1 before the maximum is raised
 
-// What a wait inside the kernel is given (about a second), besides kUnitCycles for every unit of its CTA's work, and
-// whether the ancestors of node tiles are handed over: a build for tests lowers the one and leaves out the
-// other, so that waits run out.
+// What a wait inside the kernel is given (about a second), and whether the ancestors of node tiles are handed
+// over: a build for tests lowers the one and leaves out the other, so that waits run out.
 #ifndef PSISPEC_ATTEND_WAIT_CYCLES
 #define PSISPEC_ATTEND_WAIT_CYCLES (1ll << 31)
 #endif
 #ifndef PSISPEC_ATTEND_HAND_OVER
 #define PSISPEC_ATTEND_HAND_OVER 1
 #endif
-// A unit takes up to 2000 cycles; the parts that run ahead of the tiles wait for whole segments of them, which may
-// take longer than a second.
+// What the warps that run segments ahead are given besides, for every unit of a CTA's work (which takes up to 2000
+// cycles): they wait while whole segments are worked on, which may take longer than a second. The sizes bound
+// the units. The other roles' waits are over within a tile's time (with this limit chains took 2% longer).
 constexpr long long kUnitCycles = 1 << 14;
 // The most ancestors of a node: they are followed one by one, up to four times for a tile, and the wait for
 // them has to see their end (4 x 2^18 steps of up to 2000 cycles, several times what a load takes). Lower
@@ -88,6 +88,7 @@ struct AttendParams {
   int box_log2;      // tokens of a page that one copy loads
   int tile_pages, tile_rest;  // 128 / page_size, 128 % page_size
   int ctas;
+  long long wait_cycles;  // the limit of a wait for whole segments
   float scale_log2;  // scale * log2(e)
   const int32_t* node_offsets;
   const int32_t* parent;
@@ -123,12 +124,6 @@ struct AttendWork {
 };
 constexpr int kWorkRing = 4;
 
-// What every wait looks at: whether a role has given up, and when to.
-struct AttendGuard {
-  volatile int dead;
-  long long limit;
-};
-
 template <int DP>
 struct AttendShared {
   uint64_t q_full[2], q_empty[2], kv_full[AttendCfg<DP>::kStages], kv_empty[AttendCfg<DP>::kStages];
@@ -142,7 +137,7 @@ struct AttendShared {
   uint32_t not_finite[2][2][2][4];  // per width of the pair and stream, alternating: value rows of a node tile
                                     // that are not finite
   uint32_t tmem;
-  AttendGuard guard;
+  volatile int dead;
 };
 
 template <int DP>
@@ -241,16 +236,17 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return d;
 }
 
-// Bounded wait: gives up after the guard's limit, or as soon as another role has given up. A role that gives up
+// Bounded wait: gives up after the limit, or as soon as another role has given up. A role that gives up
 // leaves its loop; copies and products that were issued are waited for (with a limit) by the warps that issued them,
 // and the second kernel makes all rows NaN.
-__device__ __forceinline__ bool attend_wait(uint64_t* bar, uint32_t parity, AttendGuard* guard) {
+__device__ __forceinline__ bool attend_wait(uint64_t* bar, uint32_t parity, volatile int* dead,
+                                            long long limit = PSISPEC_ATTEND_WAIT_CYCLES) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
-    if (guard->dead) return false;
-    if (clock64() - t0 > guard->limit) {
-      guard->dead = 1;
+    if (*dead) return false;
+    if (clock64() - t0 > limit) {
+      *dead = 1;
       return false;
     }
   }
@@ -447,7 +443,7 @@ __device__ __forceinline__ bool ancestor_bits(const int32_t* parent, int i, int 
 // A softmax warp: rows 32 wq .. 32 wq + 31 of stream s, one per lane.
 template <int DP, bool F16>
 __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShared<DP>& sh, uint8_t* tiles, uint32_t tmem,
-                                               AttendGuard* guard) {
+                                               volatile int* dead) {
   using Cfg = AttendCfg<DP>;
   const int G = p.shape.G, npt = p.shape.npt;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -461,7 +457,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
   bool ok = true;
   for (int at = 0;; ++at) {
     const AttendWork& w = sh.work[at % kWorkRing];
-    ok = __all_sync(0xffffffffu, attend_wait(&sh.w_full[at % kWorkRing], (at / kWorkRing) & 1, guard));
+    ok = __all_sync(0xffffffffu, attend_wait(&sh.w_full[at % kWorkRing], (at / kWorkRing) & 1, dead));
     if (!ok || w.last) break;
     const bool wide = w.wide;
     const int n = w.tiles, steps = wide ? n : (n + 1 - s) / 2;
@@ -481,7 +477,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
       uint32_t bits[4];
       if (is_node) {
         const int buf = n_uses & 1;
-        ok = __all_sync(0xffffffffu, attend_wait(&sh.n_full[s][buf], (n_uses >> 1) & 1, guard));
+        ok = __all_sync(0xffffffffu, attend_wait(&sh.n_full[s][buf], (n_uses >> 1) & 1, dead));
         if (!ok) break;
         ++n_uses;
         const uint4 x4 = p.seen[((blockIdx.x * 2 + s) * 2 + buf) * kTileRows + node_in];
@@ -497,7 +493,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
           bits[j] = k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
         }
       }
-      ok = __all_sync(0xffffffffu, attend_wait(&sh.s_full[s], s_uses & 1, guard));
+      ok = __all_sync(0xffffffffu, attend_wait(&sh.s_full[s], s_uses & 1, dead));
       if (!ok) break;
       ++s_uses;
       tmem_fence_after();
@@ -560,7 +556,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
       }
       if (is_node || count < kTileKeys) {  // rows of V that must not be multiplied
         const int slot = w.ring + v_slot(wide, tt, n), st = slot % Cfg::kStages;
-        ok = __all_sync(0xffffffffu, attend_wait(&sh.kv_full[st], (slot / Cfg::kStages) & 1, guard));
+        ok = __all_sync(0xffffffffu, attend_wait(&sh.kv_full[st], (slot / Cfg::kStages) & 1, dead));
         if (!ok) break;
         uint8_t* const row = tiles + (2 + st) * Cfg::kTileBytes + r * 128;
         bool drop = r >= count;
@@ -585,7 +581,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
             sh.not_finite[wide][s][buf][wq] = word;
             mbar_arrive(met);
           }
-          ok = __all_sync(0xffffffffu, attend_wait(met, use & 1, guard));
+          ok = __all_sync(0xffffffffu, attend_wait(met, use & 1, dead));
           if (!ok) break;
           ++v_uses[wide];
           const volatile uint32_t* mine = sh.not_finite[wide][s][buf];
@@ -613,7 +609,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
     const int64_t slot_row = w.row + (s ? w.rows[0] : 0) + r;
     const int64_t out_row = int64_t(w.lo + node) * p.Hq + w.kvh * G + head_in;  // of a wide pair
     if (steps > 0) {
-      ok = __all_sync(0xffffffffu, attend_wait(&sh.o_full[s], o_uses & 1, guard));
+      ok = __all_sync(0xffffffffu, attend_wait(&sh.o_full[s], o_uses & 1, dead));
       if (!ok) break;
       ++o_uses;
       tmem_fence_after();
@@ -674,7 +670,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   AttendShared<DP>& sh = *reinterpret_cast<AttendShared<DP>*>(tiles + Cfg::kTiles * Cfg::kTileBytes);
   const uint32_t q_addr = smem_u32(tiles), kv_addr = q_addr + 2 * Cfg::kTileBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  AttendGuard* const guard = &sh.guard;
+  volatile int* dead = &sh.dead;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -700,7 +696,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
     mbar_init(&sh.v_one[0], 4);
     mbar_init(&sh.v_one[1], 4);
     mbar_init(&sh.done, 1);
-    sh.guard.dead = 0;
+    sh.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -709,7 +705,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   AttendWalk walk;
   int C = 0;
   if (!attend_place<DP>(p, sh, load, walk, &C)) return;  // the same in every thread
-  if (tid == 0) sh.guard.limit = PSISPEC_ATTEND_WAIT_CYCLES + (walk.w1 - walk.w0) * kUnitCycles;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
                  : "memory");
@@ -724,11 +719,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   bool ok = true;
   // the next segment, null at the end
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, attend_wait(bar, parity, guard)) != 0;
+    return __all_sync(0xffffffffu, attend_wait(bar, parity, dead)) != 0;
   };
-  auto take = [&]() -> const AttendWork* {
+  auto wait_segments = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, attend_wait(bar, parity, dead, p.wait_cycles)) != 0;
+  };
+  auto take = [&](bool ahead = false) -> const AttendWork* {
     const int i = at % kWorkRing;
-    ok = wait_all(&sh.w_full[i], (at / kWorkRing) & 1);
+    ok = ahead ? wait_segments(&sh.w_full[i], (at / kWorkRing) & 1) : wait_all(&sh.w_full[i], (at / kWorkRing) & 1);
     return ok && !sh.work[i].last ? &sh.work[i] : nullptr;
   };
 
@@ -741,12 +739,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
       for (bool more = true; more && ok; ++at) {
         more = walk.next(seg, load);
         const int i = at % kWorkRing;
-        ok = wait_all(&sh.w_empty[i], ((at / kWorkRing) & 1) ^ 1);
+        ok = wait_segments(&sh.w_empty[i], ((at / kWorkRing) & 1) ^ 1);
         if (!ok) break;
         bool off = more && seg.g.bad;
         const int pre_tiles = more ? seg.g.pre_tiles : 0;
         auto check = [&](const int32_t* table, int t0, int t1, int len) {  // the pages that the segment reads
           const int64_t from = int64_t(t0) * kTileKeys, end = min(int64_t(len), int64_t(t1) * kTileKeys);
+#pragma unroll 4
           for (int64_t k = from / p.page_size + lane; k * p.page_size < end; k += 32) {
             const int page = __ldg(table + k);
             off |= page < 0 || page >= p.pages;
@@ -796,7 +795,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
     } else if (warp == 11) {
       // ----- nodes -----
       uint32_t uses[2] = {0, 0};
-      while (const AttendWork* w = take()) {
+      while (const AttendWork* w = take(true)) {
         const int lo = w->lo, n = w->n, first = w->first_node, t0 = w->t0, end = t0 + w->tiles;
         const bool wide = w->wide;
         const int32_t* parent = p.parent ? p.parent + lo : nullptr;
@@ -804,7 +803,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
           const int base = (t - w->ctx_tiles) * kTileKeys;
           for (int s = wide ? 0 : (t - t0) & 1; s <= (wide ? 1 : (t - t0) & 1); ++s) {
             const int buf = uses[s] & 1, from = first + (wide ? s * npt : 0), nodes = min(npt, n - from);
-            ok = wait_all(&sh.n_empty[s][buf], ((uses[s] >> 1) & 1) ^ 1);
+            ok = wait_segments(&sh.n_empty[s][buf], ((uses[s] >> 1) & 1) ^ 1);
             if (!ok) break;
             ++uses[s];
             for (int k = 0; 32 * k < nodes; ++k) {
@@ -997,12 +996,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_tree_kernel(const __
   } else {
     // ----- softmax -----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    attend_softmax<DP, F16>(p, sh, tiles, tmem, guard);
+    attend_softmax<DP, F16>(p, sh, tiles, tmem, dead);
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (tid == 0 && sh.guard.dead) p.plan->w = 1;  // gave up: the second kernel answers NaN
+  if (tid == 0 && sh.dead) p.plan->w = 1;  // gave up: the second kernel answers NaN
   if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }

@@ -192,5 +192,10 @@ inline int64_t max_items(int64_t B, int64_t N, int npt, int64_t Hkv, bool prefix
   const int64_t pairs = N / (2 * npt) + 1;
   return Hkv * (pairs + (B < N ? B : N) + (prefix ? pairs : 0));
 }
+// Of units per CTA, for keys of `tokens` in any one request besides its nodes.
+inline int64_t max_units(int64_t B, int64_t N, int npt, int64_t Hkv, int64_t tokens, int ctas) {
+  const int64_t tiles = tokens / kTileKeys + N / kTileKeys + 3;  // (of the prefix, the context and the nodes)
+  return (N / npt + (B < N ? B : N) + N / npt + 1) * Hkv * (tiles + item_cost(2)) / ctas + 2;
+}
 
 }  // namespace psi

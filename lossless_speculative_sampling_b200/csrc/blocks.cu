@@ -187,6 +187,9 @@ psispec_status attend_impl(const psispec_attend_tree_args& a, void* ws, cudaStre
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PSISPEC_ERR_CUDA;
   p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  p.wait_cycles = PSISPEC_ATTEND_WAIT_CYCLES +
+                  kUnitCycles * max_units(a.B, a.N, p.shape.npt, a.Hkv,
+                                          (int64_t(a.max_pages) + a.prefix_pages) * a.page_size, p.ctas);
   p.B = a.B;
   p.N = a.N;
   p.Hq = a.Hq;

@@ -323,11 +323,11 @@ def test_attend_tree_depth(tmp_path, monkeypatch):
 
 def test_attend_tree_long_segments_are_waited_for(tmp_path, monkeypatch):
     """Parts of the kernel that run ahead wait while whole segments are worked on, so a wait's limit has to grow
-    with the work: with waits of 2^15 cycles, several items of 8192 tokens per block (64 tiles of more than a
+    with the work: with waits of 2^16 cycles, several items of 16384 tokens per block (128 tiles of more than a
     thousand cycles each) are right all the same."""
-    lib = limited_library(tmp_path, "PSISPEC_ATTEND_WAIT_CYCLES=(1ll<<15)")
+    lib = limited_library(tmp_path, "PSISPEC_ATTEND_WAIT_CYCLES=(1ll<<16)")
     g = torch.Generator(DEV).manual_seed(93)
-    B, Hq, Hkv, D, page, ctx = 111, 16, 8, 64, 64, 8192
+    B, Hq, Hkv, D, page, ctx = 111, 16, 8, 64, 64, 16384
     q, k, v = (torch.randn(B, h, D, generator=g, device=DEV).bfloat16() for h in (Hq, Hkv, Hkv))
     kc, vc = (torch.randn(512, page, Hkv, D, generator=g, device=DEV).bfloat16() for _ in range(2))
     table = torch.randint(0, 512, (B, ctx // page), generator=g, device=DEV, dtype=torch.int32)
