@@ -373,8 +373,9 @@ psispec_status psispec_verify_linear_static(const void* target_logits, const voi
  * not matter.
  * Data errors (a token outside [0, V); a probability of a drafted token, or a value in a row that
  * the draw reads, that is negative, infinite or NaN; a drawn row without any mass; offsets out of
- * order) set that request's accept length and tokens to -1 (only the length for bad offsets).
- * draft_tokens and u_accept may be NULL when N = 0. No workspace.
+ * order) set that request's accept length and tokens to -1 (only the length for bad offsets). Offsets
+ * that step back can give two other requests the same rows: such rows of out_tokens hold the tokens of either.
+ * draft_tokens and u_accept may be NULL when N = 0. No workspace. The outputs must not overlap the inputs.
  * Limits: B >= 1, N >= 0, N + B <= 2^26, V <= 2^24, strides <= 2^32; arrays of 4-byte values start at
  * a multiple of 4.
  */
@@ -418,6 +419,7 @@ psispec_status psispec_verify_probs(const void* target_probs, int64_t target_str
  * [0, max_pages * page_size] or a page outside [0, pages) in that request (of the prefix: in every
  * request); offsets out of order in all N rows. A value of a node's v_nodes that is not finite
  * reaches the rows of that node and its descendants alone (it may turn them into NaN as a whole).
+ * The outputs must not overlap the inputs or each other.
  * One outcome is no data error: the kernel's parts wait for one another with a limit (about a second; for
  * whole stretches of work eight times what they take besides), so that a fault of the device or of this
  * library cannot hang it. If a limit passes, all rows of all requests become NaN; the call itself has returned
@@ -476,7 +478,7 @@ psispec_status psispec_attend_tree(const psispec_attend_tree_args* args, void* w
  * An accept length of -1 (a data error of the verification) commits nothing and keeps the length.
  * Data errors (an accept length or path entry outside the request's nodes, more tokens than its
  * pages hold, a page outside [0, pages)) commit nothing and give out_context_len = -1. Two
- * requests must not share a page that either writes.
+ * requests must not share a page that either writes, and the nodes must not lie in pages that are written.
  * Limits: D a multiple of 8, D, Hkv, L <= 1024, B <= 2^20, accepted nodes of a request <= 1023.
  */
 typedef struct {

@@ -26,9 +26,9 @@
 // Keys that a row does not see get the score -inf; rows of V behind a length are zeroed in shared
 // memory before they are multiplied, since their weight of 0 would not silence a NaN.
 //
-// Measured on a B200: 16 tries of 61 nodes behind 2K shared and 1K own tokens (32 heads of 128) 78 us,
-// 64 tries behind 8K 550-590 us (0.53 of the burst rate of products); 64 single tokens over 8K own
-// tokens 240 us (0.94 of the copy rate), where nothing but memory counts. In the steady state
+// Measured on a B200 (device time): 16 tries of 61 nodes behind 2K shared and 1K own tokens (32 heads of 128) 77 us,
+// 64 tries behind 8K 547-640 us (0.47 to 0.55 of the burst rate of products); 64 single tokens over 8K own
+// tokens 232-259 us (0.87 to 0.98 of the copy rate), where nothing but memory counts. In the steady state
 // a pair of 128-key tiles takes 3975 cycles: 1576 of exponentials, 1290 until the scores are there,
 // 367 for the maximum; the products of both streams need about 2050 and the exponentials 2048, so
 // each unit idles half the time, and what bounds it is that a stream has one score tile: its next

@@ -54,7 +54,11 @@ psispec_status probs_launch(const ProbArgs& a, int dev, cudaStream_t st) {
 // 110 rows of 32768 10.1 with 2 against 12.7 with 4, but 100 rows of 151936 29.1 against 25.6;
 // 200 rows of 32768 14.2 with 1 against 12.7 with 2, 230 rows 14.2 against 16.6; 512 rows of
 // 16384 18.6 with 1 against 32.3 with 4, of 151936 124 against 100 (rows of their own length
-// each then even out over four times as many CTAs).
+// each then even out over four times as many CTAs). Around the bound of 400 KB, for 223, 300, 445 and 512
+// rows: of 300 KB (bf16, 151936) 33.6, 40.0, 50.2, 63.5 with 1 against 33.0, 40.0, 55.3, 61.6 with 4; of 400 KB
+// (bf16, 204800) 43.4, 47.8, 59.6, 79.2 against 38.2, 45.6, 64.1, 72.6; of 512 KB (fp32, 131072) 42.9, 50.4, 69.7,
+// 86.0 against 38.8, 47.6, 65.8, 73.3. (2, which this rule does not take there: 29.0, 38.7, 47.3, 54.1; 36.7,
+// 47.3, 58.3, 67.0; 39.8, 50.9, 64.4, 73.3.)
 template <typename T>
 int prob_cluster(const ProbArgs& a) {
   const bool far = a.V >= (int64_t(400) << 10) / int64_t(sizeof(T));

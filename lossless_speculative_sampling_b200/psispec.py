@@ -3,7 +3,9 @@
 Argument marshalling only: torch CUDA tensors in, device pointers and sizes to the library,
 torch tensors out. Outputs and workspaces that the caller does not pass are allocated with
 torch (device memory is plumbing here); the library itself allocates nothing. Calls are
-enqueued on the current torch stream of the tensors' device (or the `stream` argument).
+enqueued on the current torch stream of the tensors' device (or the `stream` argument, a torch stream
+or a handle). As with torch's own operations, it is the caller who orders streams, and who keeps tensors
+that another stream still uses alive (or marks them with record_stream).
 
 Loading fails loudly when the library has not been built (`python -m
 lossless_speculative_sampling_b200.build`); there is no CPU fallback.
