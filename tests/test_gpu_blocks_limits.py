@@ -107,6 +107,23 @@ def test_commit_tree_refuses_a_path_without_columns():
     assert (kc == 0).all()
 
 
+def test_a_captured_call_by_handle():
+    """The handle of the stream that captures: the call and what it allocates belong to the graph."""
+    p = Problem([5, 3], [40, 20], 33, 4, 2, 64, 16, torch.bfloat16, 65)
+    args, pre = p.args()
+    psispec.attend_tree(*args, **pre)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = psispec.attend_tree(*args, **pre, stream=torch.cuda.current_stream().cuda_stream)
+    junk = [torch.full((1 << 20,), NAN, device=DEV) for _ in range(8)]
+    for t, seed in ((args[0], 66), (args[1], 67)):
+        t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(seed)))
+    del junk
+    g.replay()
+    torch.cuda.synchronize()
+    p.check(r)
+
+
 # --- a user's program ---------------------------------------------------------------------------
 
 def readme_step():
