@@ -425,7 +425,7 @@ psispec_status psispec_verify_probs(const void* target_probs, int64_t target_str
  * library cannot hang it. If a limit passes, all rows of all requests become NaN; the call itself has returned
  * PSISPEC_OK by then.
  * Limits: D a multiple of 8 up to 128, Hq / Hkv up to 128, Hkv up to 1024, page_size a multiple of 8,
- * N * Hq <= 2^22, B <= 2^20, tokens of a page table's row <= 2^30; a node with more than 2^18 ancestors counts
+ * N * Hq <= 2^22, B <= 2^20, tokens of a page table's row <= 2^30; a node with more than 2^17 ancestors counts
  * as one with a bad parent. Ancestors in parent are followed one by one: a long chain is faster with
  * parent NULL.
  */

@@ -64,11 +64,11 @@ constexpr float kRaise = 8.0f;  // log2 of how far weights may pass 1 before the
 // cycles): they wait while whole segments are worked on, which may take longer than a second. The sizes bound
 // the units. The other roles' waits are over within a tile's time (with this limit chains took 2% longer).
 constexpr long long kUnitCycles = 1 << 14;
-// The most ancestors of a node: they are followed one by one, up to four times for a tile, and the wait for
-// them has to see their end (4 x 2^18 steps of up to 2000 cycles, several times what a load takes). Lower
-// in a build for tests.
+// The most ancestors of a node: they are followed one by one, for 32 nodes at a time, so up to four times for a
+// query tile and eight for a pair, and the wait for them has to see their end (8 x 2^17 steps of up to 2000
+// cycles, several times what a load takes). Lower in a build for tests.
 #ifndef PSISPEC_ATTEND_MAX_DEPTH
-#define PSISPEC_ATTEND_MAX_DEPTH (1 << 18)
+#define PSISPEC_ATTEND_MAX_DEPTH (1 << 17)
 #endif
 
 template <int DP>
